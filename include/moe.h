@@ -536,6 +536,21 @@ typedef struct {
  * smaller one of the same K and N.  Zero its header once (moe_workspace_init);
  * one call uses it at a time. */
 MOE_API size_t moe_linear_workspace_size(const moe_linear_t* lin);
+/* How a product runs on the current device, for tests and profiles: the kernel,
+ * its tile and the parts its reduction is cut into, as a call of this shape
+ * takes them (T > 0).  has_residual and has_z say whether a forward has them.
+ *   MOE_LINEAR_SPLIT       128 output columns x `tile` rows, a cluster of `split` CTAs a tile
+ *   MOE_LINEAR_PAIR        256 output rows x `tile` columns, persistent CTA pairs
+ *   MOE_LINEAR_PAIR_SPLIT  the same tiles, a cluster of `split` pairs a tile */
+typedef enum { MOE_LINEAR_FWD = 0, MOE_LINEAR_DX = 1, MOE_LINEAR_DW = 2 } moe_linear_product_t;
+typedef enum { MOE_LINEAR_SPLIT = 0, MOE_LINEAR_PAIR = 1, MOE_LINEAR_PAIR_SPLIT = 2 } moe_linear_kernel_t;
+typedef struct {
+  int32_t kernel; /* moe_linear_kernel_t */
+  int32_t tile;
+  int32_t split;
+} moe_linear_plan_t;
+MOE_API moe_status_t moe_linear_plan(const moe_linear_t* lin, int32_t product, int32_t has_residual, int32_t has_z,
+                                     moe_linear_plan_t* plan);
 /* bias, residual and z may be NULL (none; z not wanted).  residual may be y
  * itself, with the same row distance; otherwise the outputs overlap neither
  * what is read nor one another (the same address is MOE_ERR_INVALID_ARG).

@@ -47,12 +47,16 @@ EXPORTED = ["moe_status_string", "moe_capacity", "moe_max_kept", "moe_expert_off
             "moe_mx_weights_size", "moe_quantize_weights_mx", "moe_mx_workspace_size", "moe_mx_rows",
             "moe_layer_fwd_mx", "moe_mx_part",
             "moe_few_workspace_size", "moe_layer_fwd_few",
-            "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd"]
+            "moe_linear_workspace_size", "moe_linear_plan", "moe_linear_fwd", "moe_linear_bwd"]
 
 MOE_FEW_MAX_TOKENS = 64   # tokens of moe_layer_fwd_few
 
 # activations of the linear layer (moe_activation_t)
 MOE_ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+# products and kernels of moe_linear_plan
+MOE_LINEAR_PRODUCT = {"fwd": 0, "dx": 1, "dW": 2}
+MOE_LINEAR_KERNEL = {0: "split", 1: "pair", 2: "pair_split"}
 
 # ids of moe_mx_part
 MOE_MX = {"W1": 0, "W3": 1, "W2": 2, "SF1": 3, "SF3": 4, "SF2": 5, "X8": 6, "XSF": 7, "H8": 8, "HSF": 9,
@@ -85,6 +89,10 @@ class _Config(ctypes.Structure):
 class _Linear(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("T", "K", "N", "activation")]
                 + [(n, ctypes.c_int64) for n in ("ldx", "ldw", "ldr", "ldy", "ldz", "lddy", "lddx", "lddw")])
+
+
+class _LinearPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kernel", "tile", "split")]
 
 
 _lib_handle = None
@@ -175,6 +183,8 @@ def _lib():
         lib.moe_layer_fwd_few.argtypes = [cfgp] + [P] * 13 + [P, SZ, P]
         lib.moe_linear_workspace_size.restype = SZ
         lib.moe_linear_workspace_size.argtypes = [linp]
+        lib.moe_linear_plan.restype = ctypes.c_int
+        lib.moe_linear_plan.argtypes = [linp, I32, I32, I32, ctypes.POINTER(_LinearPlan)]
         lib.moe_linear_fwd.restype = ctypes.c_int
         lib.moe_linear_fwd.argtypes = [linp] + [P] * 6 + [P, SZ, P]
         lib.moe_linear_bwd.restype = ctypes.c_int
@@ -893,6 +903,16 @@ def moe_linear_workspace_size(cfg: MoELinearConfig) -> int:
 def alloc_linear_workspace(cfg: MoELinearConfig, device=None, stream=None) -> torch.Tensor:
     """A workspace of ``moe_linear_workspace_size(cfg)`` bytes, header zeroed (torch-owned)."""
     return _alloc_init(moe_linear_workspace_size(cfg), "moe_linear_workspace_size", device, stream)
+
+
+def moe_linear_plan(cfg: MoELinearConfig, product: str, residual: bool = False, z: bool = False) -> Tuple[str, int, int]:
+    """(kernel, tile, split) of a product ("fwd", "dx" or "dW") on the current device; see moe.h."""
+    if product not in MOE_LINEAR_PRODUCT:
+        raise ValueError(f"unknown product {product!r}: one of {', '.join(MOE_LINEAR_PRODUCT)}")
+    p = _LinearPlan()
+    _check(_lib().moe_linear_plan(ctypes.byref(cfg.c()), MOE_LINEAR_PRODUCT[product], int(residual), int(z),
+                                  ctypes.byref(p)), "moe_linear_plan")
+    return MOE_LINEAR_KERNEL[p.kernel], p.tile, p.split
 
 
 def moe_linear_fwd(cfg: MoELinearConfig, x, W, bias, residual, y, ws: torch.Tensor, z=None, stream=None) -> None:

@@ -80,16 +80,42 @@ bool operand_map(CUtensorMap* m, const void* p, bool by_mn, bool* three_d, uint6
   return by_mn ? make_map(m, p, mn, red, ld, 64, 64) : make_map(m, p, red, mn, ld, 64, box);
 }
 
-// One product, by the kernel whose plan is the shorter.
+// Shape of a product: its operands' majors, lanes, columns and reduction.
+LinearArgs product_of(const moe_linear_t& l, int product) {
+  LinearArgs a{};
+  if (product == MOE_LINEAR_FWD) {  // [T, N]: lanes n, columns t, reduction k
+    a.a_mn = true;
+    a.L = l.N;
+    a.C = l.T;
+    a.red = l.K;
+  } else if (product == MOE_LINEAR_DX) {  // [T, K]: lanes k, columns t, reduction n
+    a.L = l.K;
+    a.C = l.T;
+    a.red = l.N;
+  } else {  // [K, N]: lanes n, columns k, reduction t
+    a.a_mn = a.b_mn = true;
+    a.L = l.N;
+    a.C = l.K;
+    a.red = l.T;
+  }
+  return a;
+}
+
+// Plans a product on the current device; whether it is linear_pair.cu's, the
+// kernel whose plan is the shorter.
+bool plan_product(LinearArgs& a) {
+  const LinearSlots slots = linear_slots_of_current_device();
+  const double split = plan_linear_split(a, slots), pair = plan_linear_pair(a, slots);
+  if (pair < split) a.bn = a.pair_bn;
+  return pair < split;
+}
+
 moe_status_t run_product(LinearArgs& a, void* ws, cudaStream_t s) {
   a.err = at<uint32_t>(ws, 0);
   a.wait_ctl = at<uint32_t>(ws, kWaitCtlOffset);
-  const LinearSlots slots = linear_slots_of_current_device();
-  const double split = plan_linear_split(a, slots), pair = plan_linear_pair(a, slots);
   const uint64_t L = static_cast<uint64_t>(a.L), C = static_cast<uint64_t>(a.C), R = static_cast<uint64_t>(a.red);
   CUtensorMap ma, mb, my, mz, mr;
-  if (pair < split) {
-    a.bn = a.pair_bn;
+  if (plan_product(a)) {
     if (!operand_map(&ma, a.a, a.a_mn, &a.a_3d, L, R, a.lda, a.bn / 2) ||
         !operand_map(&mb, a.b, a.b_mn, &a.b_3d, C, R, a.ldb, 128) ||
         !make_map(&my, a.out, L, C, a.ldo, 32, 32, true))
@@ -120,6 +146,24 @@ size_t moe_linear_workspace_size(const moe_linear_t* lin) {
   return linear_layout(*lin).total;
 }
 
+moe_status_t moe_linear_plan(const moe_linear_t* lin, int32_t product, int32_t has_residual, int32_t has_z,
+                             moe_linear_plan_t* plan) {
+  moe_status_t st = linear_validate(lin);
+  if (st != MOE_OK) return st;
+  if (plan == nullptr || lin->T == 0 || product < MOE_LINEAR_FWD || product > MOE_LINEAR_DW) return MOE_ERR_INVALID_ARG;
+  int sms;
+  if ((st = device_ready(&sms)) != MOE_OK) return st;
+  LinearArgs a = product_of(*lin, product);
+  // the plan asks whether these are there, not where
+  if (product == MOE_LINEAR_FWD && has_residual) a.residual = reinterpret_cast<const __nv_bfloat16*>(plan);
+  if (product == MOE_LINEAR_FWD && has_z) a.z = reinterpret_cast<__nv_bfloat16*>(plan);
+  const bool pair = plan_product(a);
+  plan->kernel = !pair ? MOE_LINEAR_SPLIT : (a.pair_split > 1 ? MOE_LINEAR_PAIR_SPLIT : MOE_LINEAR_PAIR);
+  plan->tile = a.bn;
+  plan->split = pair ? a.pair_split : a.split;
+  return MOE_OK;
+}
+
 moe_status_t moe_linear_fwd(const moe_linear_t* lin, const moe_bf16_t* x, const moe_bf16_t* W, const float* bias,
                             const moe_bf16_t* residual, moe_bf16_t* y, moe_bf16_t* z, void* ws, size_t ws_bytes,
                             void* stream) {
@@ -137,15 +181,11 @@ moe_status_t moe_linear_fwd(const moe_linear_t* lin, const moe_bf16_t* x, const 
   if ((st = linear_ws(l, ws, ws_bytes, &L)) != MOE_OK) return st;
   int sms;
   if ((st = device_ready(&sms)) != MOE_OK) return st;
-  LinearArgs a{};
+  LinearArgs a = product_of(l, MOE_LINEAR_FWD);
   a.a = bf(W);
   a.lda = ld_of(l.ldw, l.N);
-  a.a_mn = true;
   a.b = bf(x);
   a.ldb = ld_of(l.ldx, l.K);
-  a.L = l.N;
-  a.C = l.T;
-  a.red = l.K;
   a.bias = bias;
   a.residual = bf(residual);
   a.ldr = ld_of(l.ldr, l.N);
@@ -208,30 +248,22 @@ moe_status_t moe_linear_bwd(const moe_linear_t* lin, const moe_bf16_t* x, const 
       lddz = l.N;
     }
   }
-  if (dx) {  // [T, K]: lanes k, columns t, reduction n
-    LinearArgs p{};
+  if (dx) {
+    LinearArgs p = product_of(l, MOE_LINEAR_DX);
     p.a = bf(W);
     p.lda = ld_of(l.ldw, l.N);
     p.b = dz;
     p.ldb = lddz;
-    p.L = l.K;
-    p.C = l.T;
-    p.red = l.N;
     p.out = bf(dx);
     p.ldo = ld_of(l.lddx, l.K);
     if ((st = run_product(p, ws, s)) != MOE_OK) return st;
   }
-  if (dW) {  // [K, N]: lanes n, columns k, reduction t
-    LinearArgs p{};
+  if (dW) {
+    LinearArgs p = product_of(l, MOE_LINEAR_DW);
     p.a = dz;
     p.lda = lddz;
-    p.a_mn = true;
     p.b = bf(x);
     p.ldb = ld_of(l.ldx, l.K);
-    p.b_mn = true;
-    p.L = l.N;
-    p.C = l.K;
-    p.red = l.T;
     p.out = bf(dW);
     p.ldo = ld_of(l.lddw, l.N);
     if ((st = run_product(p, ws, s)) != MOE_OK) return st;

@@ -173,3 +173,17 @@ def test_linear_config_copies_and_follows_its_fields():
     for d in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
         d.T = 7
         assert d._arg(0, 0)._obj.T == 7 and c._arg(0, 0)._obj.T == 6
+
+
+def test_linear_plan_checks_its_arguments(lib):
+    p = moe._LinearPlan()
+
+    def plan(cfg, product=0, out=ctypes.byref(p)):
+        return lib.moe_linear_plan(ctypes.byref(cfg.c()), product, 0, 0, out)
+
+    assert plan(replace(LIN, K=12)) == plan(LIN, 3) == plan(LIN, -1) == moe.MOE_ERR_INVALID_ARG
+    assert plan(LIN, 0, None) == plan(replace(LIN, T=0)) == moe.MOE_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="unknown product"):
+        moe.moe_linear_plan(LIN, "dz")
+    if not torch.cuda.is_available():
+        assert [plan(LIN, i) for i in range(3)] == [moe.MOE_ERR_NO_DEVICE] * 3
