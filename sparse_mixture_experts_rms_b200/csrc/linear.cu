@@ -82,9 +82,11 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzArgs a)
 // and the eight sums are added in warp order.
 // AFTER: a product was launched between this kernel and linear_dz_kernel.  This one
 // starts once all CTAs of the product let it, which they do after their own wait for
-// what came before them, so the partial sums are complete, and it works beside the
-// product; it waits for the product before it ends, since whoever comes next waits
-// for this kernel only.
+// what came before them, so the partial sums are complete and in L2 by then, and it
+// works beside the product.  Its own wait, which would make them visible to every
+// kind of load, comes after it reads them: so it reads them from L2 (__ldcg), past an
+// L1 that may hold lines of an earlier call's sums at the same addresses.  It waits
+// for the product before it ends, since whoever comes next waits for this kernel only.
 template <bool AFTER>
 __global__ void __launch_bounds__(256) linear_dbias_kernel(const double* part, float* dbias, int N, int chunks) {
   __shared__ double sums[8][32];
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const double* part, f
   double s = 0.0;
   if (n < N) {
 #pragma unroll 8
-    for (int c = w; c < chunks; c += 8) s += part[static_cast<size_t>(c) * N + n];
+    for (int c = w; c < chunks; c += 8) s += __ldcg(part + static_cast<size_t>(c) * N + n);
   }
   sums[w][lane] = s;
   __syncthreads();

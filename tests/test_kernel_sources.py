@@ -1,0 +1,31 @@
+"""Rules of the kernels' sources that no run can show to be broken: what they order holds on the GPU either way, until a
+compiler or a chip makes use of its freedom (no GPU needed)."""
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "sparse_mixture_experts_rms_b200", "csrc")
+
+
+def source(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(src, start):
+    """The brace block that begins after `start`."""
+    i = src.index("{", src.index(start))
+    depth = 0
+    for j in range(i, len(src)):
+        depth += {"{": 1, "}": -1}.get(src[j], 0)
+        if depth == 0:
+            return src[i:j]
+    raise AssertionError(start)
+
+
+def test_sums_read_before_the_kernels_own_wait_come_from_l2():
+    """linear_dbias_kernel<true> reads the column sums before its griddepcontrol.wait: only by loads that pass L1."""
+    kernel = body(source("linear.cu"), "linear_dbias_kernel(")
+    assert "if (AFTER) griddep_wait()" in kernel and kernel.index("part") < kernel.rindex("griddep_wait")
+    assert re.findall(r"\bpart\b", kernel) and re.findall(r"\bpart\b", kernel) == re.findall(r"(?<=__ldcg\()part\b", kernel)
