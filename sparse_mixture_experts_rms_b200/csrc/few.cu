@@ -436,10 +436,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           const int row0 = sh.tab.rows[p.e], ne = rows_of(sh.tab, p.e), n8 = (ne + 7) & ~7;
           if (!ready) {
             // H of the line's experts is complete when all tiles of their up line are
-            int got = 1;
-            if (lane == 0)
-              got = few_wait_word(&a.done[li - 2], sh.line[li - 2].tiles, abort_flag, a.err, wait_ns) ? 1 : 0;
-            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
+            bool got = true;
+            if (lane == 0) got = few_wait_word(&a.done[li - 2], sh.line[li - 2].tiles, abort_flag, a.err, wait_ns);
+            if (!warp_take(got)) {
               go = false;
               break;
             }
@@ -459,13 +458,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
           for (int k = p.k0; k < p.k1; ++k, ++it) {
             const int s = it % S;
-            int got = 1;
+            bool got = true;
             if (lane == 0) {
-              got = mbar_wait(&sh.empty[s], ((it / S) & 1u) ^ 1u, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns)
-                        ? 1 : 0;
+              got = mbar_wait(&sh.empty[s], ((it / S) & 1u) ^ 1u, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns);
               if (got) mbar_arrive_expect_tx(&sh.full_b[s], tx);
             }
-            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
+            if (!warp_take(got)) {
               go = false;
               break;
             }

@@ -731,11 +731,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const int s = it % kStages;
         const uint32_t ph = (it / kStages) & 1u;
-        int got = 1;
+        bool got = true;
         if (lane == 0)
-          got = mbar_wait(&sh.empty[s], ph ^ 1u, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns, false, peer_abort)
-                    ? 1 : 0;
-        if (!__shfl_sync(0xFFFFFFFFu, got, 0)) {
+          got = mbar_wait(&sh.empty[s], ph ^ 1u, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns, false, peer_abort);
+        if (!warp_take(got)) {
           ok = false;
           break;
         }
@@ -854,7 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(EPI), 1)
       bool ok = true;
       if (lane == 0)
         ok = mbar_wait(&sh.tfull[buf], aph, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns, false, peer_abort);
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+      ok = warp_take(ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;

@@ -388,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       if (lane == 0)
         ok = mbar_wait(&sh.tfull[buf], aph, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns, false, peer_abort);
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+      ok = warp_take(ok);
       if (!ok) break;
       tc_fence_after();
       epilogue(a, sh, c, tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf_col(buf), row_in_cta, rank, buf,

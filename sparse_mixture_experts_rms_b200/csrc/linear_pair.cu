@@ -334,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FULL>::kThreads,
       if (lane == 0)
         got = mbar_wait(&sh.tfull[buf], (tcount >> 1) & 1u, abort_flag, a.err, MOE_DEVERR_TIMEOUT, wait_ns, false,
                         peer_abort);
-      ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+      ok = warp_take(got);
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols + c_lo;
       int i = 0;
@@ -347,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FULL>::kThreads,
         if (has_res) {
           got = true;
           if (lane == 0) got = res_wait(i, abort_flag, wait_ns);
-          ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+          ok = warp_take(got);
         } else {
           // the store that used this slot last has read it
           if (lane == 0) bulk_wait_group_read_allow(static_cast<int>(slots) - 1);

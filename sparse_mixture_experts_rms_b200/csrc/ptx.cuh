@@ -98,6 +98,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The result of a wait that lane 0 made for its warp, for every lane.  A shuffle
+// orders no memory; the barrier behind it puts what lane 0's wait acquired before
+// whatever the other lanes do next (their copies, their reads of what has landed).
+__device__ __forceinline__ bool warp_take(bool got) {
+  const bool r = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+  __syncwarp();
+  return r;
+}
+
 // Decrement the pending transaction bytes of the current phase of `bar`
 // without a copy (for bytes that were expected but will never be sent).
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {

@@ -345,10 +345,9 @@ __global__ void __launch_bounds__(RouteCfg<EP>::kThreads, 1)
           // the other warp of the quarter holds the rest of each row
           if (lane == 0) mbar_arrive(&sh.xg_ready[q]);
           if (half == 0) {
-            int got = 1;
-            if (lane == 0)
-              got = mbar_wait(&sh.xg_ready[q], st & 1u, abort_flag, err, MOE_DEVERR_TIMEOUT, wait_ns) ? 1 : 0;
-            stored = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+            bool got = true;
+            if (lane == 0) got = mbar_wait(&sh.xg_ready[q], st & 1u, abort_flag, err, MOE_DEVERR_TIMEOUT, wait_ns);
+            stored = warp_take(got);
           }
         }
         if (stored && half == 0 && lane == 0 && t0 + q * 32 < a.T) {

@@ -29,3 +29,15 @@ def test_sums_read_before_the_kernels_own_wait_come_from_l2():
     kernel = body(source("linear.cu"), "linear_dbias_kernel(")
     assert "if (AFTER) griddep_wait()" in kernel and kernel.index("part") < kernel.rindex("griddep_wait")
     assert re.findall(r"\bpart\b", kernel) and re.findall(r"\bpart\b", kernel) == re.findall(r"(?<=__ldcg\()part\b", kernel)
+
+
+def test_a_wait_made_by_one_lane_is_shared_with_a_barrier():
+    """A shuffle orders no memory: a wait's result reaches the other lanes through warp_take, whose barrier does."""
+    assert "__syncwarp()" in body(source("ptx.cuh"), "bool warp_take(")
+    files = [f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    assert len(files) > 10
+    for f in files:
+        src = source(f).replace(body(source(f), "bool warp_take("), "") if f == "ptx.cuh" else source(f)
+        assert not re.search(r"__shfl_sync\(\w+,\s*(got|ok)\b", src), f
+    for f in ("few.cu", "linear_pair.cu"):
+        assert source(f).count("warp_take(") == 2, f
