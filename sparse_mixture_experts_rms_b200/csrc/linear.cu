@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(256, 4) linear_dz_kernel(const LinearDzArgs a)
     int terms = 0;
     uint4 g[AHEAD], z[HAS_Z ? AHEAD : 1];
     auto load = [&](int r, int s) {
-      g[s] = r < row_end ? __ldg(reinterpret_cast<const uint4*>(a.dy + r * a.lddy + col)) : zero;
-      if (HAS_Z) z[s] = r < row_end ? __ldg(reinterpret_cast<const uint4*>(a.z + r * a.ldz + col)) : zero;
+      g[s] = r < row_end ? ld_global16(a.dy + r * a.lddy + col) : zero;
+      if (HAS_Z) z[s] = r < row_end ? ld_global16(a.z + r * a.ldz + col) : zero;
     };
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s) load(row_first + 8 * s, s);

@@ -19,6 +19,22 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Loads of what the kernel before may have written while this one was already
+// starting: `ld.global.nc` (__ldg) is for memory that nobody writes while the kernel
+// runs.  As asm they keep its freedom to move past the kernel's own stores, though
+// not past griddep_wait; plain loads made linear_dz_kernel spill (16384 x 14336 of
+// SiLU 181 -> 193 us).
+__device__ __forceinline__ uint4 ld_global16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_global(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // Two fp32 in a register pair: one instruction adds, multiplies or
 // multiply-adds both.
 using f32x2 = unsigned long long;
@@ -218,7 +234,7 @@ __device__ __forceinline__ void finish_groups(const LinearArgs& a, const int (&c
     res[u] = in[u] && a.residual != nullptr ? *reinterpret_cast<const uint2*>(a.residual + c[u] * a.ldr + l[u])
                                             : make_uint2(0u, 0u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * u + j] = in[u] && a.bias != nullptr ? __ldg(a.bias + l[u] + j) : 0.f;
+    for (int j = 0; j < 4; ++j) v[4 * u + j] = in[u] && a.bias != nullptr ? ld_global(a.bias + l[u] + j) : 0.f;
   }
   float sum[4 * U];
 #pragma unroll

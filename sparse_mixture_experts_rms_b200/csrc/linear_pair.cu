@@ -317,16 +317,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<FULL>::kThreads,
         if (bias_wide) {  // whole groups of 8 columns lie inside or outside the matrix
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (col + j < a.L) b = __ldg(reinterpret_cast<const float4*>(a.bias + col + j));
-            bias[j] = b.x;
-            bias[j + 1] = b.y;
-            bias[j + 2] = b.z;
-            bias[j + 3] = b.w;
+            uint4 b = make_uint4(0u, 0u, 0u, 0u);
+            if (col + j < a.L) b = ld_global16(a.bias + col + j);
+            bias[j] = __uint_as_float(b.x);
+            bias[j + 1] = __uint_as_float(b.y);
+            bias[j + 2] = __uint_as_float(b.z);
+            bias[j + 3] = __uint_as_float(b.w);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) bias[j] = col + j < a.L ? __ldg(a.bias + col + j) : 0.f;
+          for (int j = 0; j < 32; ++j) bias[j] = col + j < a.L ? ld_global(a.bias + col + j) : 0.f;
         }
       };
       if (has_bias && chunks > 0) load_bias(col0);

@@ -41,3 +41,11 @@ def test_a_wait_made_by_one_lane_is_shared_with_a_barrier():
         assert not re.search(r"__shfl_sync\(\w+,\s*(got|ok)\b", src), f
     for f in ("few.cu", "linear_pair.cu"):
         assert source(f).count("warp_take(") == 2, f
+
+
+def test_linear_kernels_read_without_the_read_only_path():
+    """The linear kernels start while the kernel before may still be writing dy, z or the bias: no `ld.global.nc`
+    (__ldg), which is for memory that nobody writes while the kernel runs."""
+    for f in ("linear.cu", "linear.cuh", "linear_split.cu", "linear_pair.cu"):
+        src = source(f)
+        assert "__ldg(" not in src and "global.nc" not in src and "__restrict__" not in src, f
