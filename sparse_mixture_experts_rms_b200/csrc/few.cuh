@@ -288,8 +288,9 @@ __device__ __forceinline__ void few_add_slices(const FewArgs& a, double* sums, d
 
 // Logits, softmax and top-k of every token into the tables (and, by CTA 0,
 // into the caller's copies).  An expert's slot is the number of experts that
-// come before it -- a larger logit, or an equal one and
-// a lower index -- so the k slots are found at once; NaN counts as -inf.
+// come before it -- a larger logit, or an equal one and a lower index -- so the k
+// slots are found at once.  A NaN compares with nothing: a token with one takes
+// the router's own k scans, in which it wins only as the first expert still free.
 __device__ __forceinline__ void few_pick(const FewArgs& a, FewTables& tab, float* r_s, uint8_t* smem) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nsl = few_slices(a), E = a.E;
   constexpr int kWarps = kFewThreads / 32;
@@ -306,7 +307,7 @@ __device__ __forceinline__ void few_pick(const FewArgs& a, FewTables& tab, float
     const int t = t0 + lane / lanes;
     const bool live = t < a.T;
     const double rv = rs[live ? t : 0];
-    float l[2], key[2], ex[2], m = -INFINITY;
+    float l[2], ex[2], m = -INFINITY;
     int before[2] = {0, 0};
     float sum = 0.f, gsum = 0.f;
     __syncwarp();
@@ -314,8 +315,7 @@ __device__ __forceinline__ void few_pick(const FewArgs& a, FewTables& tab, float
     for (int h = 0; h < 2; ++h) {
       const int e = el + 32 * h;
       l[h] = e < E && live ? static_cast<float>(fma(rv, sums[t * E + e], static_cast<double>(tab.bias[e]))) : -INFINITY;
-      key[h] = l[h] == l[h] ? l[h] : -INFINITY;
-      if (h == 0 || E > 32) lg[e] = key[h];
+      if (h == 0 || E > 32) lg[e] = l[h];
       m = fmaxf(m, l[h]);
     }
     for (int q = lanes >> 1; q > 0; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, q));
@@ -328,8 +328,20 @@ __device__ __forceinline__ void few_pick(const FewArgs& a, FewTables& tab, float
 #pragma unroll 4
     for (int e = 0; e < E; ++e) {
       const float o = lg[e];
-      before[0] += o > key[0] || (o == key[0] && e < el);
-      before[1] += o > key[1] || (o == key[1] && e < el + 32);
+      before[0] += o > l[0] || (o == l[0] && e < el);
+      before[1] += o > l[1] || (o == l[1] && e < el + 32);
+    }
+    if (__any_sync(0xFFFFFFFFu, l[0] != l[0] || l[1] != l[1])) {
+      uint64_t used = 0;
+      before[0] = before[1] = a.k;
+      for (int j = 0; j < a.k; ++j) {
+        int best = -1;
+        for (int e = 0; e < E; ++e)
+          if (!((used >> e) & 1u) && (best < 0 || lg[e] > lg[best])) best = e;
+        used |= uint64_t(1) << best;
+        if (best == el) before[0] = j;
+        if (best == el + 32) before[1] = j;
+      }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -339,7 +351,8 @@ __device__ __forceinline__ void few_pick(const FewArgs& a, FewTables& tab, float
       gsum += __shfl_xor_sync(0xFFFFFFFFu, gsum, q);
     }
     if (!live) continue;
-    const float inv = 1.0f / (a.renormalize ? gsum : sum);
+    // a NaN among the logits makes every gate one, renormalised or not: 0 * sum
+    const float inv = 1.0f / (a.renormalize ? gsum + 0.f * sum : sum);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int e = el + 32 * h;
