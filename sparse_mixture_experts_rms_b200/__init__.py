@@ -974,6 +974,8 @@ class _MoELinearFn(torch.autograd.Function):
         dbias = torch.empty((cfg.N,), dtype=torch.float32, device=x.device) if need_b else None
         if need_x or need_w or need_b:
             g = dy.to(torch.bfloat16).contiguous()
+            if g.data_ptr() % 16:  # a contiguous view may start anywhere
+                g = g.clone()
             moe_linear_bwd(cfg, x, W, z, g, dx, dW, dbias, ctx.layer._plan(x)[1])
         return None, None, dx, dW, dbias, dy if need_r else None
 
