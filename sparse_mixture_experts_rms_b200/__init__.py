@@ -842,7 +842,8 @@ class MoEFewLayer:
     weights and one workspace; ``forward(x)`` calls moe_layer_fwd_few.  The
     tokens of a call may be fewer than ``cfg.T`` (the rows of x say how many);
     cfg is read when the layer is made.  Calls share the workspace, so they
-    belong on one stream."""
+    belong on one stream.  There is no backward: a call through which a gradient
+    would have to pass is refused (torch.no_grad(), or MoETrainLayer)."""
 
     def __init__(self, cfg: MoEConfig, gamma, Wr, bias, W1, W3, W2):
         self.cfg = replace(cfg)
@@ -861,6 +862,11 @@ class MoEFewLayer:
         return c[1]
 
     def forward(self, x, residual=None, out=None, expert_idx=None, gate=None, r=None, counts=None, stream=None):
+        if torch.is_grad_enabled() and (
+                x.requires_grad or (residual is not None and residual.requires_grad) or self.W1.requires_grad
+                or self.W3.requires_grad or self.W2.requires_grad or self.gamma.requires_grad or self.Wr.requires_grad
+                or (self.bias is not None and self.bias.requires_grad)):
+            raise RuntimeError("MoEFewLayer has no backward: call it under torch.no_grad(), or train with MoETrainLayer")
         if out is None:
             out = torch.empty_like(x)
         _few(self._config(x.shape[0]), self.cfg.F, x, self.gamma, self.Wr, self.bias, self.W1, self.W3, self.W2, out,
