@@ -846,7 +846,7 @@ class MoEFewLayer:
     would have to pass is refused (torch.no_grad(), or MoETrainLayer)."""
 
     def __init__(self, cfg: MoEConfig, gamma, Wr, bias, W1, W3, W2):
-        self.cfg = replace(cfg)
+        self.cfg = replace(cfg, ffn_offsets=list(cfg.ffn_offsets))
         self.gamma, self.Wr, self.bias = gamma, Wr, bias
         self.W1, self.W3, self.W2 = W1, W3, W2
         self.ws = alloc_few_workspace(cfg, device=gamma.device)

@@ -187,3 +187,16 @@ def test_linear_plan_checks_its_arguments(lib):
         moe.moe_linear_plan(LIN, "dz")
     if not torch.cuda.is_available():
         assert [plan(LIN, i) for i in range(3)] == [moe.MOE_ERR_NO_DEVICE] * 3
+
+
+def test_few_layer_keeps_its_own_configuration(monkeypatch):
+    """cfg is read when the layer is made: what its owner does to it (or to its list of offsets) later reaches no call."""
+    monkeypatch.setattr(moe, "alloc_few_workspace", lambda cfg, device=None, stream=None: None)
+    t = torch.zeros(1)
+    cfg = replace(CFG, T=8, ffn_offsets=list(CFG.ffn_offsets))
+    layer = moe.MoEFewLayer(cfg, t, t, None, t, t, t)
+    before = list(layer._config(3).ffn_offsets[0:9])
+    cfg.ffn_offsets[1:8] = [256, 384, 512, 640, 768, 896, 960]
+    cfg.T, cfg.k = 1, 1
+    assert list(layer._config(3).ffn_offsets[0:9]) == before
+    assert list(layer._config(7).ffn_offsets[0:9]) == before and layer._config(7).k == 2
