@@ -536,6 +536,10 @@ typedef struct {
  * smaller one of the same K and N.  Zero its header once (moe_workspace_init);
  * one call uses it at a time. */
 MOE_API size_t moe_linear_workspace_size(const moe_linear_t* lin);
+/* Bytes that moe_linear_fwd alone asks for (0 if invalid): 4 KB, whatever the
+ * shape, since dz and the column sums are the backward's.  A larger workspace
+ * serves too. */
+MOE_API size_t moe_linear_fwd_workspace_size(const moe_linear_t* lin);
 /* How a product runs on the current device, for tests and profiles: the kernel,
  * its tile and the parts its reduction is cut into, as a call of this shape
  * takes them (T > 0).  has_residual and has_z say whether a forward has them.

@@ -47,7 +47,8 @@ EXPORTED = ["moe_status_string", "moe_capacity", "moe_max_kept", "moe_expert_off
             "moe_mx_weights_size", "moe_quantize_weights_mx", "moe_mx_workspace_size", "moe_mx_rows",
             "moe_layer_fwd_mx", "moe_mx_part",
             "moe_few_workspace_size", "moe_layer_fwd_few",
-            "moe_linear_workspace_size", "moe_linear_plan", "moe_linear_fwd", "moe_linear_bwd"]
+            "moe_linear_workspace_size", "moe_linear_fwd_workspace_size", "moe_linear_plan", "moe_linear_fwd",
+            "moe_linear_bwd"]
 
 MOE_FEW_MAX_TOKENS = 64   # tokens of moe_layer_fwd_few
 
@@ -183,6 +184,8 @@ def _lib():
         lib.moe_layer_fwd_few.argtypes = [cfgp] + [P] * 13 + [P, SZ, P]
         lib.moe_linear_workspace_size.restype = SZ
         lib.moe_linear_workspace_size.argtypes = [linp]
+        lib.moe_linear_fwd_workspace_size.restype = SZ
+        lib.moe_linear_fwd_workspace_size.argtypes = [linp]
         lib.moe_linear_plan.restype = ctypes.c_int
         lib.moe_linear_plan.argtypes = [linp, I32, I32, I32, ctypes.POINTER(_LinearPlan)]
         lib.moe_linear_fwd.restype = ctypes.c_int
@@ -906,9 +909,15 @@ def moe_linear_workspace_size(cfg: MoELinearConfig) -> int:
     return int(_lib().moe_linear_workspace_size(ctypes.byref(cfg.c())))
 
 
-def alloc_linear_workspace(cfg: MoELinearConfig, device=None, stream=None) -> torch.Tensor:
-    """A workspace of ``moe_linear_workspace_size(cfg)`` bytes, header zeroed (torch-owned)."""
-    return _alloc_init(moe_linear_workspace_size(cfg), "moe_linear_workspace_size", device, stream)
+def moe_linear_fwd_workspace_size(cfg: MoELinearConfig) -> int:
+    return int(_lib().moe_linear_fwd_workspace_size(ctypes.byref(cfg.c())))
+
+
+def alloc_linear_workspace(cfg: MoELinearConfig, device=None, stream=None, forward_only: bool = False) -> torch.Tensor:
+    """A workspace of ``moe_linear_workspace_size(cfg)`` bytes (``forward_only``: of the few that moe_linear_fwd alone
+    asks for, which serve any shape), header zeroed (torch-owned)."""
+    size = moe_linear_fwd_workspace_size if forward_only else moe_linear_workspace_size
+    return _alloc_init(size(cfg), size.__name__, device, stream)
 
 
 def moe_linear_plan(cfg: MoELinearConfig, product: str, residual: bool = False, z: bool = False) -> Tuple[str, int, int]:
@@ -958,7 +967,9 @@ class _MoELinearFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, layer, training, x, W, bias, residual):
-        cfg, ws = layer._plan(x)
+        K, N = W.shape
+        cfg = MoELinearConfig(T=x.shape[0], K=K, N=N, activation=layer.activation)
+        ws = layer._fwd_ws(cfg)
         y = torch.empty((cfg.T, cfg.N), dtype=torch.bfloat16, device=x.device)
         z = torch.empty_like(y) if training and cfg.activation != "none" else None
         moe_linear_fwd(cfg, x, W, bias, residual, y, ws, z=z)
@@ -982,34 +993,42 @@ class _MoELinearFn(torch.autograd.Function):
             g = dy.to(torch.bfloat16).contiguous()
             if g.data_ptr() % 16:  # a contiguous view may start anywhere
                 g = g.clone()
-            moe_linear_bwd(cfg, x, W, z, g, dx, dW, dbias, ctx.layer._plan(x)[1])
+            moe_linear_bwd(cfg, x, W, z, g, dx, dW, dbias, ctx.layer._bwd_ws(cfg))
         return None, None, dx, dW, dbias, dy if need_r else None
 
 
 class MoELinear:
     """A linear layer y = act(x W + bias) + residual with its gradients by
     autograd: W [K, N] bf16, bias [N] fp32 or None, x and residual bf16 [T, .]
-    with any T.  Calls share a workspace, so they belong on one stream; it grows
-    by powers of two of T, and those it outgrew are kept, since a captured graph
-    may hold them.  A forward without gradients can be captured once a call of
-    as many rows has been made.  With gradients, capture moe_linear_fwd and
+    with any T.  Calls share a workspace, so they belong on one stream.  The
+    forward's is 4 KB, made by the first call and kept, since a captured graph
+    may hold it; the backward's scratch (about T N bf16 values) is made by the
+    first backward and replaced when one needs more.  A forward without
+    gradients can be captured, with any T, once a call has been made; the layer
+    must outlive the graph.  With gradients, capture moe_linear_fwd and
     moe_linear_bwd instead: autograd's nodes remember the stream they were made
     on, so a capture of them is refused."""
 
     def __init__(self, W, bias=None, activation: str = "none"):
         self.W, self.bias, self.activation = W, bias, activation
-        self._T, self._ws = 0, []  # rows that the last workspace holds
+        self._ws = self._scratch = None
+        self._scratch_of = (0, 0, 0)  # T, K, N that the scratch is for
 
-    def _plan(self, x):
-        K, N = self.W.shape
-        cfg = MoELinearConfig(T=x.shape[0], K=K, N=N, activation=self.activation)
-        if not self._ws or cfg.T > self._T:
+    def _fwd_ws(self, cfg):
+        if self._ws is None:
             if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError(f"MoELinear: call it with {cfg.T} rows once before capturing it")
-            T = 1 << max(cfg.T - 1, 0).bit_length()
-            self._ws.append(alloc_linear_workspace(replace(cfg, T=T), device=self.W.device))
-            self._T = T
-        return cfg, self._ws[-1]
+                raise RuntimeError("MoELinear: call it once before capturing it")
+            self._ws = alloc_linear_workspace(cfg, device=self.W.device, forward_only=True)
+        return self._ws
+
+    def _bwd_ws(self, cfg):
+        T, K, N = self._scratch_of
+        if cfg.T > T or cfg.K != K or cfg.N != N or self._scratch is None:
+            self._scratch = alloc_linear_workspace(cfg, device=self.W.device)
+            self._scratch_of = cfg.T, cfg.K, cfg.N
+        # one that is replaced goes back to the allocator: not before this stream is done with it
+        self._scratch.record_stream(torch.cuda.current_stream(self._scratch.device))
+        return self._scratch
 
     def forward(self, x, residual=None):
         leaves = (x, self.W, self.bias)

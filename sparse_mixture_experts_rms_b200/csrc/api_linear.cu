@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxLd = int64_t(1) << 38;  // a TMA row distance is below 2^40 bytes
 constexpr int32_t kMaxExtent = 1 << 30;       // tile arithmetic is 32-bit
+constexpr size_t kFwdBytes = 4096;            // the forward's workspace: the header, and room for more like it
 
 struct LinearLayout {
   size_t part, dz, total;
@@ -53,13 +54,12 @@ LinearLayout linear_layout(const moe_linear_t& l) {
   L.chunk_rows = (l.T + L.chunks - 1) / L.chunks;
   L.part = take(static_cast<size_t>(L.chunks) * l.N * 8);
   L.dz = take(static_cast<size_t>(l.T) * l.N * 2);
-  L.total = off;
+  L.total = std::max(off, kFwdBytes);
   return L;
 }
 
-moe_status_t linear_ws(const moe_linear_t& l, void* ws, size_t ws_bytes, LinearLayout* L) {
-  *L = linear_layout(l);
-  if (ws == nullptr || ws_bytes < L->total) return MOE_ERR_WORKSPACE;
+moe_status_t linear_ws(void* ws, size_t ws_bytes, size_t needed) {
+  if (ws == nullptr || ws_bytes < needed) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
   return MOE_OK;
 }
@@ -146,6 +146,10 @@ size_t moe_linear_workspace_size(const moe_linear_t* lin) {
   return linear_layout(*lin).total;
 }
 
+size_t moe_linear_fwd_workspace_size(const moe_linear_t* lin) {
+  return linear_validate(lin) == MOE_OK ? kFwdBytes : 0;
+}
+
 moe_status_t moe_linear_plan(const moe_linear_t* lin, int32_t product, int32_t has_residual, int32_t has_z,
                              moe_linear_plan_t* plan) {
   moe_status_t st = linear_validate(lin);
@@ -177,8 +181,7 @@ moe_status_t moe_linear_fwd(const moe_linear_t* lin, const moe_bf16_t* x, const 
     return MOE_ERR_ALIGNMENT;
   if (same(y, {x, W, z}) || same(z, {x, W, residual})) return MOE_ERR_INVALID_ARG;
   if (residual == y && l.T > 1 && ld_of(l.ldr, l.N) != ld_of(l.ldy, l.N)) return MOE_ERR_INVALID_ARG;
-  LinearLayout L;
-  if ((st = linear_ws(l, ws, ws_bytes, &L)) != MOE_OK) return st;
+  if ((st = linear_ws(ws, ws_bytes, kFwdBytes)) != MOE_OK) return st;
   int sms;
   if ((st = device_ready(&sms)) != MOE_OK) return st;
   LinearArgs a = product_of(l, MOE_LINEAR_FWD);
@@ -222,8 +225,8 @@ moe_status_t moe_linear_bwd(const moe_linear_t* lin, const moe_bf16_t* x, const 
   if (!dy || (has_act && !z) || (dx && !W) || (dW && !x)) return MOE_ERR_INVALID_ARG;
   if (same(dx, {x, W, z, dy, dW}) || same(dW, {x, W, z, dy}) || same(dbias, {x, W, z, dy, dx, dW}))
     return MOE_ERR_INVALID_ARG;
-  LinearLayout L;
-  if ((st = linear_ws(l, ws, ws_bytes, &L)) != MOE_OK) return st;
+  const LinearLayout L = linear_layout(l);
+  if ((st = linear_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
   if ((st = device_ready(&sms)) != MOE_OK) return st;
   const __nv_bfloat16* dz = bf(dy);
   int64_t lddz = ld_of(l.lddy, l.N);

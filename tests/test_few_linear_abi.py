@@ -200,3 +200,19 @@ def test_few_layer_keeps_its_own_configuration(monkeypatch):
     cfg.T, cfg.k = 1, 1
     assert list(layer._config(3).ffn_offsets[0:9]) == before
     assert list(layer._config(7).ffn_offsets[0:9]) == before and layer._config(7).k == 2
+
+
+def test_linear_forward_asks_for_a_workspace_without_the_backwards_scratch(lib):
+    big = moe.MoELinearConfig(T=16384, K=4096, N=14336, activation="silu")
+    n = moe.moe_linear_fwd_workspace_size(big)
+    assert n == moe.moe_linear_fwd_workspace_size(LIN) == 4096
+    assert moe.moe_linear_workspace_size(big) > 16384 * 14336 * 2
+    assert moe.moe_linear_workspace_size(LIN) >= n            # a workspace of the layer serves its forward
+    bad = LIN.c()
+    bad.K = 12
+    assert lib.moe_linear_fwd_workspace_size(ctypes.byref(bad)) == 0
+    fine = moe.MOE_OK if torch.cuda.is_available() else moe.MOE_ERR_NO_DEVICE
+    if fine != moe.MOE_OK:                                    # (with a device the call would run, on these pointers)
+        assert fwd(lib, big.c(), n=n) == fine
+    assert fwd(lib, big.c(), n=n - 1) == moe.MOE_ERR_WORKSPACE
+    assert bwd(lib, big.c(), n=n) == moe.MOE_ERR_WORKSPACE
