@@ -85,6 +85,7 @@ moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const moe_bf16_t* x, con
   if (!aligned(ws, 256)) return MOE_ERR_ALIGNMENT;
   if ((st = device_ready(&sms)) != MOE_OK) return st;
   const moe_config_t& c = *cfg;
+  if (sms < c.T) return MOE_ERR_UNSUPPORTED;  // few_route: a CTA takes one token's slice
   FewArgs a{};
   a.x = reinterpret_cast<const __nv_bfloat16*>(x);
   a.gamma = reinterpret_cast<const __nv_bfloat16*>(gamma);

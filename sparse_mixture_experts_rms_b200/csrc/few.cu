@@ -564,7 +564,6 @@ cudaError_t launch_few(FewArgs& a, const CUtensorMap& map1, const CUtensorMap& m
   a.stages = static_cast<int>((kSmemMax - fixed) / stage);
   if (a.stages > kFewMaxStages) a.stages = kFewMaxStages;
   if (a.stages < 2 || a.stages * stage < static_cast<int>(kFewScratchBytes)) return cudaErrorInvalidValue;
-  if (sms < a.T) return cudaErrorInvalidConfiguration;  // a CTA routes at most one token
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms < kFewMaxGrid ? sms : kFewMaxGrid));
   cfg.blockDim = dim3(kFewThreads);

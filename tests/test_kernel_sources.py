@@ -49,3 +49,13 @@ def test_linear_kernels_read_without_the_read_only_path():
     for f in ("linear.cu", "linear.cuh", "linear_split.cu", "linear_pair.cu"):
         src = source(f)
         assert "__ldg(" not in src and "global.nc" not in src and "__restrict__" not in src, f
+
+
+def test_a_device_with_too_few_sms_is_told_so():
+    """The few-token kernel needs an SM a token.  No GPU here has fewer than 64, so the check is read: it gives the
+    documented status, before the launch."""
+    call = body(source("api_few.cu"), "moe_status_t moe_layer_fwd_few(")
+    check = call.index("if (sms < c.T) return MOE_ERR_UNSUPPORTED;")
+    assert call.index("device_ready(&sms)) != MOE_OK) return st;\n  const moe_config_t& c") < check < call.index("launch_few(")
+    with open(os.path.join(ROOT, "include", "moe.h")) as f:
+        assert "with fewer than T SMs" in f.read()
