@@ -31,10 +31,10 @@
 // activations lose nothing that the formula's fp32 would keep visible in the
 // bf16 output.
 //
-// Measured (device time of a call in a graph; floor = the chosen experts' bytes at
-// the 6.55 TB/s of a copy): 8 experts of 4096 x 14336, top-2, one token (705 MB)
-// 123 us against 107, 64 tokens (2.8 GB) 449 against 430; 7 tokens of 64 experts
-// of 2048 x 512, top-8, 58 us against 37, where the chain of dependent steps
+// Measured (device time of a call in a graph, by the GPU; floor = the chosen experts'
+// bytes at the 6.55 TB/s of a copy): 8 experts of 4096 x 14336, top-2, one token
+// (705 MB) 122-126 us against 107, 64 tokens (2.8 GB) 447-460 against 430; 7 tokens of 64
+// experts of 2048 x 512, top-8, 55-58 us against 37, where the chain of dependent steps
 // shows: routing 3.5 us, choice and tables 3.3, first tile 3, from the last up
 // tile to the first down stage about 8, combine and its wait 3.  DRAM reads are
 // the weights' bytes to 0.1 %.

@@ -86,8 +86,9 @@ __device__ __forceinline__ f32x2 magnitude2(f32x2 z) {
 }
 // Phi(-|z|) / e^(-z^2/2) = erfcx(|z| / sqrt 2) / 2 for the normal distribution's
 // Phi: a polynomial without constant term in t = 1 / (1 + 0.35 |z|), fitted to
-// the smallest largest relative error over 0 <= |z| <= 14 (beyond, e^(-z^2/2)
-// is zero in fp32); 3.1e-8, a few fp32 roundings as evaluated.
+// a small largest relative error over 0 <= |z| <= 14 (beyond, e^(-z^2/2) is zero in
+// fp32): 6.0e-8 with these coefficients in exact arithmetic, reached at both
+// ends; the evaluation in fp32 adds a few roundings of that size.
 __device__ __forceinline__ f32x2 phi_ratio2(f32x2 az) {
   const f32x2 t = rcp_pair(fma2(both(0.35f), az, both(1.0f)));
   f32x2 p = both(-0.02914595790207386f);

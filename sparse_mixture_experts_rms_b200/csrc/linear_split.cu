@@ -21,9 +21,10 @@
 // adds them in rank order, applies the epilogue and stores.  No workspace, no
 // counters, and a fixed order of every sum.
 //
-// Measured (device time in a graph): one row of 4096 x 4096 10.1 us (33.6 MB of W:
-// 5.1 us at a copy's rate; the rest is launch, first loads and exchange), 61 rows of
-// 1000 x 2056 7.9 us, 500 rows of 1024 x 4096 10.9 us (386 TFLOP/s).
+// Measured (device time in a graph, by the GPU and its clock): one row of 4096 x 4096
+// 8.3-10.2 us (33.6 MB of W: 5.1 us at a copy's rate; the rest is launch, first loads
+// and exchange), 61 rows of 1000 x 2056 6.9-7.9 us, 700 rows of 4096 x 1024 14.0-16.5 us
+// (360-420 TFLOP/s).
 //
 // Warps: 0 = TMA, 1 = MMA issue and TMEM, 2-5 = TMEM to shared memory, then all
 // of them the epilogue, 4 lanes (8 bytes of output) a thread.
@@ -208,9 +209,11 @@ __global__ void __launch_bounds__(kThreads)
       finish_groups<U>(a, c, l, in, from, S, 0u, 1u);
     }
   };
-  // with few groups the code to fetch is what counts (one row of 4096 x 4096: 8.9 us, 9.2 with two
-  // a thread and 10.3 with four), with many the loads under way (128 rows of 4096 x 14336: 32.9 us
-  // with one, 29.9 with two)
+  // with few groups the code to fetch is what counts, with many the loads under way: one against two
+  // groups a thread 8.3 and 8.8 us for one row of 4096 x 4096 (2 columns a rank), 10.1 and 10.8 for dx of
+  // 157 x 1056 x 2328 (10 columns), 12.2 and 12.6 at 16 columns (128 x 4096 x 4096); but 14.4 and 14.0 at 22
+  // (700 x 4096 x 1024), 7.6 and 7.1 at 27 (303 x 464 x 1288), 15.0 and 13.4 at 59 (523 x 1912 x 1704).
+  // (Four a thread: 10.3 us for the one row.)
   if (items <= 2 * kThreads)
     finish(std::integral_constant<int, 1>{});
   else
