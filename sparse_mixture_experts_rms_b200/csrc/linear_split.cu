@@ -23,7 +23,7 @@
 //
 // Measured (device time in a graph, by the GPU and its clock): one row of 4096 x 4096
 // 8.3-10.2 us (33.6 MB of W: 5.1 us at a copy's rate; the rest is launch, first loads
-// and exchange), 61 rows of 1000 x 2056 6.9-7.9 us, 700 rows of 4096 x 1024 14.0-16.5 us
+// and exchange), 61 rows of 1000 x 2056 6.7-7.9 us, 700 rows of 4096 x 1024 14.0-16.5 us
 // (360-420 TFLOP/s).
 //
 // Warps: 0 = TMA, 1 = MMA issue and TMEM, 2-5 = TMEM to shared memory, then all
