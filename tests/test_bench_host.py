@@ -80,3 +80,11 @@ def test_l2_flush_rule_follows_the_layer_footprint():
     assert not bench.flushes_l2(W["fine_grained"])
     assert "flushed" in bench.workload_config(W["tiny"], 1)["l2"]
     assert "no flush" in bench.workload_config(m, 1)["l2"]
+
+
+def test_measured_traffic_is_of_these_kernels():
+    """The bench line gives the up GEMM's DRAM bytes only while the sources that they were measured on stand: a change
+    to them takes a new capture (profiles/grouped_gemm_traffic_mixtral_T16384.md has the command)."""
+    assert bench.MEASURED_TRAFFIC["digest"] == bench.kernel_digest()
+    with open(os.path.join(ROOT, "profiles", "grouped_gemm_traffic_mixtral_T16384.md")) as f:
+        assert bench.kernel_digest() in f.read().split("\n\n")[1]
