@@ -486,9 +486,9 @@ MOE_API int64_t moe_train_rows(const moe_config_t* cfg);
  *   expert_idx, gate, r, counts: optional copies of the routing, as in
  *            moe_layer_fwd.
  * T > MOE_FEW_MAX_TOKENS is MOE_ERR_UNSUPPORTED, and so is a device (a slice of
- * one) with fewer than T SMs: a CTA routes one token at most.  The result does not depend on
- * the order in which CTAs run: the same inputs give the same bits.  The
- * workspace is used by one call at a time (calls on one stream follow one
+ * one) with fewer than T SMs: a CTA routes one token at most.  The result does
+ * not depend on the order in which CTAs run: the same inputs give the same bits.
+ * The workspace is used by one call at a time (calls on one stream follow one
  * another; two graphs that share it must not overlap); its header must have
  * been zeroed once by moe_workspace_init, and a workspace of a larger T serves
  * a smaller one.  The kernel occupies every SM once and its CTAs wait on one

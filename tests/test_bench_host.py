@@ -84,7 +84,7 @@ def test_l2_flush_rule_follows_the_layer_footprint():
 
 def test_measured_traffic_is_of_these_kernels():
     """The bench line gives the up GEMM's DRAM bytes only while the sources that they were measured on stand: a change
-    to them takes a new capture (profiles/grouped_gemm_traffic_mixtral_T16384.md has the command)."""
+    to them takes a new capture, whose record gives the digest too."""
     assert bench.MEASURED_TRAFFIC["digest"] == bench.kernel_digest()
     with open(os.path.join(ROOT, "profiles", "grouped_gemm_traffic_mixtral_T16384.md")) as f:
         assert bench.kernel_digest() in f.read().split("\n\n")[1]
