@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
-  griddep_wait();  // y and inv_perm come from the kernels before
+  griddep_wait();  // y and inv_perm come from the kernels before (so: no ld.global.nc)
   const int lane = threadIdx.x & 31;
   const int warps = (gridDim.x * blockDim.x) >> 5;
   const int chunks = a.d / 8;
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
         for (int jj = 0; jj < nj; ++jj) {
           const int pos = __shfl_sync(0xFFFFFFFFu, mine, jj);
           if (pos >= 0 && c < chunks) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.y + static_cast<size_t>(pos) * a.d) + c);
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.y + static_cast<size_t>(pos) * a.d) + c);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

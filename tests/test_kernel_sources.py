@@ -43,10 +43,10 @@ def test_a_wait_made_by_one_lane_is_shared_with_a_barrier():
         assert source(f).count("warp_take(") == 2, f
 
 
-def test_linear_kernels_read_without_the_read_only_path():
-    """The linear kernels start while the kernel before may still be writing dy, z or the bias: no `ld.global.nc`
-    (__ldg), which is for memory that nobody writes while the kernel runs."""
-    for f in ("linear.cu", "linear.cuh", "linear_split.cu", "linear_pair.cu"):
+def test_dependent_launches_read_without_the_read_only_path():
+    """The linear kernels and the combine start while the kernel before may still be writing dy, z, the bias or y: no
+    `ld.global.nc` (__ldg), which is for memory that nobody writes while the kernel runs."""
+    for f in ("linear.cu", "linear.cuh", "linear_split.cu", "linear_pair.cu", "combine.cu"):
         src = source(f)
         assert "__ldg(" not in src and "global.nc" not in src and "__restrict__" not in src, f
 
