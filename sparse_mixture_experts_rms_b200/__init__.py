@@ -679,6 +679,12 @@ class MoELayer:
     __call__ = forward
 
 
+def _upstream(g):
+    """An upstream gradient as the library takes it: bf16, dense rows, 16-byte aligned."""
+    g = g.to(torch.bfloat16).contiguous()
+    return g.clone() if g.data_ptr() % 16 else g  # a contiguous view may start anywhere
+
+
 class _MoETrainFn(torch.autograd.Function):
     """autograd glue: forward = moe_layer_fwd_train, backward = moe_layer_bwd.
     Gradients come back in fp32 and are cast to each input's dtype."""
@@ -702,7 +708,7 @@ class _MoETrainFn(torch.autograd.Function):
         g = [torch.empty((T, d), **f32), torch.empty((d,), **f32), torch.empty((d, E), **f32),
              torch.empty((E,), **f32), torch.empty((d, F), **f32), torch.empty((d, F), **f32),
              torch.empty((F, d), **f32)]
-        moe_layer_bwd(cfg, x, gamma, Wr, bias, W1, W3, W2, dout.to(torch.bfloat16).contiguous(), *g, tws)
+        moe_layer_bwd(cfg, x, gamma, Wr, bias, W1, W3, W2, _upstream(dout), *g, tws)
         dx, dgamma, dWr, dbias, dW1, dW3, dW2 = g
         return (None, None, dx.to(x.dtype), dgamma.to(gamma.dtype), dWr.to(Wr.dtype),
                 dbias if ctx.has_bias else None, dW1.to(W1.dtype), dW3.to(W3.dtype), dW2.to(W2.dtype))
@@ -990,10 +996,7 @@ class _MoELinearFn(torch.autograd.Function):
         dW = torch.empty((cfg.K, cfg.N), **bf) if need_w else None
         dbias = torch.empty((cfg.N,), dtype=torch.float32, device=x.device) if need_b else None
         if need_x or need_w or need_b:
-            g = dy.to(torch.bfloat16).contiguous()
-            if g.data_ptr() % 16:  # a contiguous view may start anywhere
-                g = g.clone()
-            moe_linear_bwd(cfg, x, W, z, g, dx, dW, dbias, ctx.layer._bwd_ws(cfg))
+            moe_linear_bwd(cfg, x, W, z, _upstream(dy), dx, dW, dbias, ctx.layer._bwd_ws(cfg))
         return None, None, dx, dW, dbias, dy if need_r else None
 
 

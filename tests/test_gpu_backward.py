@@ -186,3 +186,18 @@ def test_degenerate_rows_backward():
     w = mw.Workload("bwd_degenerate", T=256, d_model=256, E=8, k=2, expert_sizes=((8, 128),))
     _, _, G = run_case(w, problem=H.degenerate_problem(w))
     assert torch.count_nonzero(G["dx"][0:16]).item() == 0
+
+
+def test_upstream_gradient_off_its_alignment():
+    """A gradient is legal wherever it starts: that of a flattened concatenation begins 2 bytes off a 16-byte boundary.
+    The same bits as from an aligned one."""
+    p = H.make_problem(mw.Workload("off", T=40, d_model=256, E=4, k=2, expert_sizes=((4, 128),)))
+    d = H.Dev(p, H.make_cfg(p))
+    x = d.x.clone().requires_grad_(True)
+    layer = moe.MoETrainLayer(d.cfg, d.gamma, d.Wr, d.bias, d.W1, d.W3, d.W2)
+    dout = H.bits_to_dev(_upstream(40, 256))
+    layer(x).backward(dout)
+    want, x.grad = x.grad.clone(), None
+    head = torch.zeros(1, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    torch.cat([head, layer(x).flatten()]).backward(torch.cat([dout.flatten()[:1], dout.flatten()]))
+    assert torch.equal(x.grad, want)
